@@ -218,9 +218,9 @@ __global__ void __launch_bounds__(kSel) select_kernel(const __grid_constant__ Kv
         // [lo, hi]: where the border lies; a key above hi stays, one below lo goes
         const bool none = need == 0;
         bool all_in = false;               // every key >= lo stays
-        for (int pass = 0; need; ++pass) {
+        for (int pass = 0; need && pass < kv_border_passes(kLogBins); ++pass) {
             const unsigned range = hi - lo;
-            const int bits = range ? 32 - __clz(range) : 0, shift = bits > kLogBins ? bits - kLogBins : 0;
+            const int shift = kv_border_shift(range, kLogBins);
             unsigned* const h = hist[pass & 1];
             unsigned* const gs = sums[pass & 1];
             for (int i = s0 + 4 * tid; i < s1; i += 4 * kSel) {
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kSel) select_kernel(const __grid_constant__ Kv
                 break;
             }
             if (shift == 0) break;         // equal keys
-            hi = min(hi, lo + ((1u << shift) - 1));
+            hi = kv_border_end(lo, hi, shift);
         }
         // Slots are numbered in strips, one a thread: as many fours as the slice needs, an odd number (no bank twice).
         const int fours = min(kStrip / 4, ((s1 - s0 + 4 * kSel - 1) / (4 * kSel)) | 1), strip = 4 * fours;

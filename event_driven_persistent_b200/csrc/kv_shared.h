@@ -93,6 +93,26 @@ KV_HD uint32_t kv_weight_key(uint32_t bits) {
     return (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
 }
 
+// The search of an eviction's border key: a pass counts the keys of [lo, hi] in at most 2^log_bins bins of 2^shift keys,
+// the first one from lo on, and the next pass takes the bin that the border lies in.
+KV_HD int kv_border_shift(uint32_t range, int log_bins) {  // range: hi - lo
+    int bits = 0;
+#ifdef __CUDA_ARCH__
+    bits = 32 - __clz((int)range);
+#else
+    while (bits < 32 && range >> bits) ++bits;
+#endif
+    return bits > log_bins ? bits - log_bins : 0;
+}
+// passes that a search takes at most: each leaves log_bins bits fewer
+KV_HD constexpr int kv_border_passes(int log_bins) { return (32 + log_bins - 1) / log_bins; }
+// the last key of the bin that begins at lo, of [lo, hi]: bins begin at any key, so the top one may pass 32 bits (a NaN's
+// key is the last there is), and only the distance from lo can be compared
+KV_HD uint32_t kv_border_end(uint32_t lo, uint32_t hi, int shift) {
+    const uint32_t step = (1u << shift) - 1;
+    return lo + (hi - lo < step ? hi - lo : step);
+}
+
 struct KvAppendParams {
     KvPool pool;
     KvTable table;

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kSel) select_kernel(const __grid_constant__ Kv
                     if (lane >= o) inc += y;
                 }
                 const unsigned before = above + inc - d;
-                if (lane == 0) {           // were weights written meanwhile, there may be no such bin: the search ends
+                if (lane == 0) {           // were weights written meanwhile, there may be no such bin: the search ends (and is reported below)
                     found[0] = 0;
                     found[1] = found[2] = need;
                 }
@@ -347,12 +347,13 @@ __global__ void __launch_bounds__(kSel) select_kernel(const __grid_constant__ Kv
             at = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? o[2] : 0u);
             ties = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? o[3] : 0u);
         }
+        const unsigned at0 = at, ties0 = ties;
         for (int first = s0;;) {
             const unsigned tb = ties + before.y, room = need > tb ? need - tb : 0u;
             while ((unsigned)__popc(m.y) > room) m.y &= ~(1u << (31 - __clz(m.y)));  // the first `room` ties
             int to = at + before.x + min(tb, need);
             for (unsigned stay = m.x | m.y; stay; stay &= stay - 1, ++to)
-                if (to < p.budget) kept[to] = i + __ffs(stay) - 1;  // (it always is, unless weights are written meanwhile)
+                if (to < p.budget) kept[to] = i + __ffs(stay) - 1;  // (it always is, unless what is checked below fails)
             at += all.x;
             ties += all.y;
             first += strip * kSel;
@@ -361,6 +362,12 @@ __global__ void __launch_bounds__(kSel) select_kernel(const __grid_constant__ Kv
             m = kinds(i);
             before = cta_scan<kSel>(count(m), tmp2, &all);
         }
+        // Keys beyond what the CTA holds are read for each step anew.  Were weights written meanwhile, the steps saw different
+        // ones: each slice has to number as many slots as it told the others, and all of them `budget`, or the entries of
+        // kept are not all written and the move must not use them.
+        if (tid == 0 && ((cs > 1 && (at - at0 != share[2] || ties - ties0 != share[3])) ||
+                         (rank == cs - 1 && at + min(ties, need) != (unsigned)p.budget)))
+            fail(p.ctl, KV_BAD_WEIGHT, b, u, (int)(at + min(ties, need)));
         if (cs > 1) cluster_sync();        // nobody leaves while another reads its shared memory
     }
     if (j0 < n_dst) claimed(j0, page0, own0);
@@ -427,7 +434,7 @@ __global__ void __launch_bounds__(kMove, 4) move_kernel(const __grid_constant__ 
             long long f = -1, t = -1, wf = 0;
             if (j < keep) {
                 const int i = kept[j];
-                // (a slot that no kept one was written to, were weights written meanwhile: nothing is moved)
+                // (the selection has written every entry, in ascending order, or reported that it has not)
                 if ((unsigned)i < (unsigned)p.src.max_len && (!IN_PLACE || i != j)) {
                     t = where(p.dst, j, false, &wt);
                     f = where(p.src, i, true, &wf);

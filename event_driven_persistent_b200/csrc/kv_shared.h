@@ -32,7 +32,7 @@ struct KvCtl {
     unsigned evict_done;     // CTAs of the eviction's last kernel that are done
 };
 // diag[0] of a KvCtl: what was out of range
-enum { KV_BAD_LEN = 1, KV_BAD_PAGE = 2, KV_BAD_REQ = 3, KV_BAD_SLOT = 4, KV_BAD_DST = 5 };
+enum { KV_BAD_LEN = 1, KV_BAD_PAGE = 2, KV_BAD_REQ = 3, KV_BAD_SLOT = 4, KV_BAD_DST = 5, KV_BAD_WEIGHT = 6 };
 
 // The pages: element (page, head, slot, d) of K and V lies at
 // page * page_stride + head * head_stride + slot * slot_stride + d (elements).

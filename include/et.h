@@ -540,7 +540,9 @@ et_status et_run_kv_attn(et_kv* kv, const et_kv_pool* pool, const et_kv_attn_arg
  * request of the run holds.  Each destination page may be named once; in
  * place, a page that new slots are written to may belong to one request only (requests
  * that keep all their slots may share pages).  The run finds
- * other tables (ET_ERR_INVALID; what was to move is then not defined).
+ * other tables (ET_ERR_INVALID; what was to move is then not defined).  So it
+ * does if weights that another stream writes meanwhile lead its steps to
+ * different choices: then nothing moves.
  * new_lens int32 [B] (may be lens): min(lens[b], budget); kept int32 [B,
  * n_kv_heads, budget]: the old slot of each new one, -1 past new_lens[b].
  * 1 <= budget, n_recent + n_sink <= budget. */
@@ -559,7 +561,8 @@ et_status et_run_kv_evict(et_kv* kv, const et_kv_pool* pool, const et_kv_evict_a
 
 /* Synchronise `stream`; read and clear the handle's error.  diag4 (host, or
  * NULL): what was out of range (1 length, 2 page, 3 request, 4 slot, 5 page named
- * twice) and where: for 3 and 4 the row, else the request. */
+ * twice, 6 weights written while an eviction read them) and where: for 3 and 4
+ * the row, else the request. */
 et_status et_sync_kv(et_kv* kv, void* stream, int32_t* diag4);
 
 #ifdef __cplusplus

@@ -148,6 +148,11 @@ __global__ void __launch_bounds__(kSel) select_kernel(const __grid_constant__ Kv
     if (n <= p.budget) {
         for (int j = rank * kSel + tid; j < n; j += cs * kSel) kept[j] = j;
         if (j0 < n_dst) own0 = claim(j0, page0);
+        if (!p.in_place) {  // nobody reads the weights of its source pages, which are as many as its destinations: here they are checked
+            const int* const pages = p.src.pages + (long long)b * p.src.ld;
+            for (int j = j0; j < n_dst; j += gridDim.x * kSel)
+                if ((unsigned)pages[j] >= (unsigned)p.pool.n_pages) fail(p.ctl, KV_BAD_PAGE, b, j * p.pool.page_size, pages[j]);
+        }
     } else {
         const int c0 = p.n_sink, c1 = n - p.n_recent;  // the slots that compete
         const int per = ((n + cs - 1) / cs + 3) & ~3, s0 = min(n, rank * per), s1 = min(n, s0 + per);

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kSel) select_kernel(const __grid_constant__ Kv
     };
     const int page0 = j0 < n_dst ? dst[j0] : 0;
     unsigned long long own0 = 0;
-    for (int j = keep + rank * kSel + tid; j < p.budget; j += cs * kSel) kept[j] = -1;
+    for (unsigned j = keep + rank * kSel + tid; j < (unsigned)p.budget; j += cs * kSel) kept[j] = -1;  // (unsigned: a budget near 2^31)
     if (n <= p.budget) {
         for (int j = rank * kSel + tid; j < n; j += cs * kSel) kept[j] = j;
         if (j0 < n_dst) own0 = claim(j0, page0);

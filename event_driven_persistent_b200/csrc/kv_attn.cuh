@@ -705,6 +705,7 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
             // a CTA with more to do leaves it, and joining a few parts, to one warp; its others go on
             if (!solo && w != (cur.u & (W - 1))) continue;
             if (!__shfl_sync(0xFFFFFFFFu, lane == 0 ? arrived_last(arr, n_parts) : 0, 0)) continue;
+            __syncwarp();  // what lane 0's arrival made visible to it is so for the others too; a shuffle alone orders no memory
             mt = lane;
             many = 32;
         } else if (n_parts <= kKvJoin) {

@@ -33,8 +33,9 @@
 // probabilities enter the second product as two 16-bit terms, high and
 // remainder (16 bits or more of p together), so that rounding p adds nothing next to
 // the output's own rounding; with up to four heads a group the remainder
-// rides in the columns that would be padding.  With an e4m3 cache and bf16
-// outputs the high term alone is fp16: 2^-11 of p, next to the output's 2^-8.  An e4m3 cache is widened to
+// rides in the columns that would be padding.  (One fp16 term, 2^-11 of p, where an e4m3 cache meets bf16
+// outputs would show where values cancel; it is no faster up to 8 heads a group, 112 against 113 us for the
+// 8 x 20000..65000 below, and 97 against 112 us with 16 heads of 128.)  An e4m3 cache is widened to
 // fp16 exactly; bf16 queries are then scaled by a power of two into fp16's range.
 //
 // Measured (32 query and 8 KV heads of 128 in bf16, pages of 16, unless said; a
@@ -130,7 +131,6 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
     // Probabilities are held as 2^up exp(x - m): fp16 operands keep their steps down to 2^(-24 - up), so that a long
     // tail of tiny ones is not lost next to one that is near 1 (bf16 has fp32's range).
     constexpr float UP = std::is_same<M, Fp16>::value ? 12.f : 0.f;
-    constexpr bool REST = !(E4 && std::is_same<T, Bf16>::value);  // a second term of p: not where fp16's 11 bits meet a bf16 output
     constexpr float SLACK = std::is_same<M, Fp16>::value ? 3.f : 8.f;  // 2^(UP + SLACK) is inside fp16
     extern __shared__ __align__(128) unsigned char smem[];
     float* join = reinterpret_cast<float*>(smem + S::kRing);
@@ -481,16 +481,12 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
                         l[n][0] += a;
                         l[n][1] += c1;
                         const uint32_t hi = M::pack(a, c1);
-                        if constexpr (!REST) {
-                            ph[i][n][h] = movm(hi);
+                        const uint32_t rest = M::pack(a - M::lo(hi), c1 - M::hi(hi));
+                        if constexpr (MODE == kCols4) {  // columns 4..7 repeat heads 0..3 and carry the remainders
+                            ph[i][n][h] = movm(t4 < 2 ? hi : rest);
                         } else {
-                            const uint32_t rest = M::pack(a - M::lo(hi), c1 - M::hi(hi));
-                            if constexpr (MODE == kCols4) {  // columns 4..7 repeat heads 0..3 and carry the remainders
-                                ph[i][n][h] = movm(t4 < 2 ? hi : rest);
-                            } else {
-                                ph[i][n][h] = movm(hi);
-                                pl[i][n][h] = movm(rest);
-                            }
+                            ph[i][n][h] = movm(hi);
+                            pl[i][n][h] = movm(rest);
                         }
                     }
             }
@@ -511,7 +507,7 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 M::mma(o[k + h][n], a, ph[i][n][0], ph[i][n][1]);
-                                if constexpr (REST && MODE != kCols4) M::mma(o[k + h][n], a, pl[i][n][0], pl[i][n][1]);
+                                if constexpr (MODE != kCols4) M::mma(o[k + h][n], a, pl[i][n][0], pl[i][n][1]);
                             }
                         }
                     }
@@ -524,7 +520,7 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             M::mma(o[k][n], a, ph[i][n][0], ph[i][n][1]);
-                            if constexpr (REST && MODE != kCols4) M::mma(o[k][n], a, pl[i][n][0], pl[i][n][1]);
+                            if constexpr (MODE != kCols4) M::mma(o[k][n], a, pl[i][n][0], pl[i][n][1]);
                         }
                     }
                 }
@@ -551,7 +547,7 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
                     sm_l[w * 16 + n * 8 + 2 * t4 + v] = l[n][v];
                 }
             }
-        if constexpr (REST && MODE == kCols4) {
+        if constexpr (MODE == kCols4) {
 #pragma unroll
             for (int k = 0; k < KK; ++k)
 #pragma unroll

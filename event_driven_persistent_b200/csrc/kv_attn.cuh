@@ -91,35 +91,6 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
     return (uint32_t)(r * ROW + ((c ^ (r & 7)) << 4));
 }
 
-// A segment, and its tiles counted from the first number of the team's run.
-struct Walk {
-    int i, u, nt;         // request (in the list of those that have tiles), unit, tiles of the segment
-    int s0, s1;           // [s0, s1): the segment's tiles
-};
-// the segment whose tiles, or the `extra` numbers before them, hold number t0
-__device__ __forceinline__ void walk_to(Walk& w, const int* pre, int live, int extra, int units, long long t0) {
-    w.i = find_request(pre, live, extra, units, t0);
-    w.nt = pre[w.i + 1] - pre[w.i];
-    const int r = (int)(t0 - (long long)(pre[w.i] + w.i * extra) * units);
-    w.u = r / (w.nt + extra);
-    w.s0 = w.u * (w.nt + extra) + extra - r;
-    w.s1 = w.s0 + w.nt;
-}
-// the next one; past the last segment it lies beyond every run
-__device__ __forceinline__ void walk_next(Walk& w, const int* pre, int live, int extra, int units) {
-    w.s0 = w.s1 + extra;
-    if (++w.u == units) {
-        w.u = 0;
-        if (++w.i == live) {
-            w.s0 = 0x7FFFFFF0;
-            w.nt = 0;
-        } else {
-            w.nt = pre[w.i + 1] - pre[w.i];
-        }
-    }
-    w.s1 = w.s0 + w.nt;
-}
-
 template <int HD, class T, int CACHE, int MODE>
 __global__ void __launch_bounds__(kKvAttnWarps * 32, (AttnShape<HD, CACHE, MODE>::kPerSm))
 attn_kernel(const __grid_constant__ KvAttnParams p) {
@@ -157,19 +128,13 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
         }
     if (live.n == 0) return;
 
-    // ---- teams: a warp each, or a CTA each.  Numbers are shared out, not tiles: a segment has `extra` numbers before
-    // its tiles, which stand for what its end costs (its join and the next one's start).
-    const long long n1 = (long long)(pre[live.n] + live.n * p.warp_extra) * units;
-    const int C1 = kv_share_teams(n1, gridDim.x * W, p.warp_share_log);
-    const bool solo = (long long)(live.longest + p.warp_extra) * C1 <= (long long)p.warp_parts * n1;
+    // ---- teams: a warp each, or a CTA each
+    const KvTeams teams = kv_choose_teams(pre[live.n], live.n, live.longest, units, gridDim.x, W, p.warp_share_log, p.cta_share_log,
+                                          p.warp_extra, p.cta_extra, p.warp_parts);
+    const bool solo = teams.solo;
     const int team = solo ? 1 : W, tw = solo ? 0 : w, tt = solo ? lane : tid;
-    const int extra = solo ? p.warp_extra : p.cta_extra;
-    const long long N = solo ? n1 : (long long)(pre[live.n] + live.n * extra) * units;
-    int C = solo ? C1 : kv_share_teams(N, gridDim.x, p.cta_share_log);
-    // requests of one length: whole teams a segment, if few idle for it (a team with two segments takes twice as
-    // long in a small run: 1 x 517 11 -> 8 us)
-    const int segs = live.n * units;
-    if (N == (long long)(live.longest + extra) * segs && C >= segs && C % segs * 8 <= C) C -= C % segs;
+    const int extra = teams.extra, C = teams.C;
+    const long long N = teams.N;
     const int c = solo ? w * gridDim.x + blockIdx.x : blockIdx.x;
     if (c >= C) return;
     auto team_sync = [&]() {
@@ -186,9 +151,9 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
     const char* const k_lane = static_cast<const char*>(p.pool.K) + (lane / CPR) * row_step + (lane % CPR) * 16;
     const long long v_off = static_cast<const char*>(p.pool.V) - static_cast<const char*>(p.pool.K);
     const bool wide = (p.page_groups & 1) == 0;  // pages of 16 rows or more: every other group lies behind the one before
-    Walk lw;
-    walk_to(lw, pre, live.n, extra, units, t0);
-    Walk seg = lw;                         // the segment in use; the loads run ahead of it
+    KvWalk lw;
+    kv_walk_to(lw, pre, live.n, extra, units, t0);
+    KvWalk seg = lw;                         // the segment in use; the loads run ahead of it
     int lt = tw;                           // next tile to load
     int lb = 0, l_len = -1;                // its request, its length, page numbers, KV head's byte offset
     const int* l_pages = nullptr;
@@ -203,7 +168,7 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
             if (lt < lw.s0) lt = lw.s0 + ((tw - lw.s0) & (team - 1));
             if (lt >= run) return;
             if (lt < lw.s1) break;
-            walk_next(lw, pre, live.n, extra, units);
+            kv_walk_next(lw, pre, live.n, extra, units);
             l_len = -1;
         }
         if (l_len < 0) {
@@ -531,9 +496,9 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
         }
 
         // ---- join the team's warps, the next segment's queries on their way meanwhile
-        const Walk cur = seg;
+        const KvWalk cur = seg;
         const int cb = b, ckvh = kvh, ch0 = h0, cnh = nh;
-        walk_next(seg, pre, live.n, extra, units);
+        kv_walk_next(seg, pre, live.n, extra, units);
         const bool more = seg.s0 < run;
         if (more) take();
 #pragma unroll
@@ -611,14 +576,13 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
 
         // ---- a shared segment: the team that arrives last joins the parts
         if (whole) continue;
-        const int c0 = (int)kv_share_owner(t0 + cur.s0, N, C), c1 = (int)kv_share_owner(t0 + cur.s1 - 1, N, C);
-        const int first = kv_share_slot(c0, t0 + cur.s0, N, C), n_parts = c1 - c0 + 1;
-        // the slot of part k
-        auto slot_of = [&](int k) { return (long long)(c0 + k) * kKvMaxSplits + (k == 0 ? first : 0); };
+        const KvParts parts = kv_parts(t0 + cur.s0, t0 + cur.s1, N, C);
+        const int n_parts = parts.n;
+        auto slot_of = [&](int k) { return kv_part_slot(parts, k); };
         // Joins `count` parts, P at a time, of 8 / P pieces of a row (their loads in flight together), with `many` threads, of
         // which this is number mt: into the output, or, unscaled, into slot `to`.  Part k lies in slot where(k).
-        auto join_parts = [&](auto parts, int count, auto where, int mt, int many, long long to) {
-            constexpr int P = decltype(parts)::value, R = 8 / P;
+        auto join_parts = [&](auto at_a_time, int count, auto where, int mt, int many, long long to) {
+            constexpr int P = decltype(at_a_time)::value, R = 8 / P;
             const int total = cnh * HD / 4;
             for (int i0 = mt; i0 < total; i0 += many * R) {
                 float mm[R], ll[R];
@@ -707,11 +671,11 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
         } else if (n_parts <= kKvJoin) {
             if (!__syncthreads_or(tid == 0 ? arrived_last(arr, n_parts) : 0)) continue;
         } else {
-            // Many parts (few segments): by groups of kKvJoin, each joined by its last arrival into a slot past the teams' own
-            // (a CTA may do so for two segments), then the groups (1 x 73306, 2 KV heads: 38 -> 24 us).
-            const int groups = (n_parts + kKvJoin - 1) / kKvJoin, gr = (c - c0) / kKvJoin, size = min(kKvJoin, n_parts - gr * kKvJoin);
+            // Many parts (few segments): by groups of kKvJoin, each joined by its last arrival into a slot past the teams'
+            // own, then the groups (1 x 73306, 2 KV heads: 38 -> 24 us).
+            const int groups = kv_join_groups(n_parts), gr = (c - parts.c0) / kKvJoin, size = min(kKvJoin, n_parts - gr * kKvJoin);
             if (!__syncthreads_or(tid == 0 ? arrived_last(arr + 1 + gr, size) : 0)) continue;
-            const long long mine = (long long)gridDim.x * kKvMaxSplits + slot;
+            const long long mine = kv_group_slot(gridDim.x, slot);
             join_parts(integral_constant<int, 8>(), size, [&](int k) { return slot_of(gr * kKvJoin + k); }, tid, W * 32, mine);
             int* const group_slot = p.group_slots + ((long long)cb * units + cur.u) * p.arrivals_ld;
             if (tid == 0) group_slot[gr] = (int)mine;

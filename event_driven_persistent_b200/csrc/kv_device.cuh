@@ -199,15 +199,6 @@ __device__ __forceinline__ Live scan_tiles(int* pre, uint16_t* id, int* tmp, con
     r.longest = most;
     return r;
 }
-// largest i < live with (pre[i] + i extra) units <= t: the request of numbered tile t
-__device__ __forceinline__ int find_request(const int* pre, int live, int extra, int units, long long t) {
-    int lo = 0, hi = live;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)(pre[mid] + mid * extra) * units <= t) lo = mid; else hi = mid;
-    }
-    return lo;
-}
 
 // Launch with programmatic serialisation: the grid may be set up while the
 // one before it drains; every kernel here calls grid_wait() before it reads

@@ -158,12 +158,12 @@ et_status build(et_kv* kv) {
         turns[i] = pow((double)d.rope_base, -2.0 * i / d.head_dim) / 6.283185307179586476925;
     KV_TRY(kv_alloc(kv, &kv->turns, turns.size()));
     KV_CU(cudaMemcpy(kv->turns, turns.data(), turns.size() * sizeof(double), cudaMemcpyHostToDevice));
-    const size_t slots = (size_t)2 * kv->n_sm * kKvAttnWarps * kKvMaxSplits;  // two CTAs an SM at most
+    const size_t slots = (size_t)kv_part_slots(kv->n_sm);
     const int group = d.n_heads / d.n_kv_heads;
     const size_t cols = group <= 4 ? 4 : (group <= 8 ? 8 : kv_unit_heads(d.head_dim, d.cache_dtype == ET_E4M3));
     KV_TRY(kv_alloc(kv, &kv->part, slots * cols * d.head_dim));
     KV_TRY(kv_alloc(kv, &kv->part_ml, slots * cols));
-    kv->arrivals_ld = 1 + (2 * kv->n_sm + kKvJoin - 1) / kKvJoin;
+    kv->arrivals_ld = kv_arrivals(kv->n_sm);
     kv->n_arrivals = (size_t)d.max_B * d.n_kv_heads * kv->n_qt * kv->arrivals_ld;
     KV_TRY(kv_alloc(kv, &kv->arrivals, kv->n_arrivals));
     KV_TRY(kv_alloc(kv, &kv->group_slots, kv->n_arrivals));
@@ -313,11 +313,10 @@ et_status et_run_kv_attn(et_kv* kv, const et_kv_pool* pool, const et_kv_attn_arg
     // the rounded-up reciprocal is exact: i < 2^21 + 8, page_groups <= 512 (1 has none in 32 bits and needs none)
     p.page_groups = d.page_size % 8 ? 0 : d.page_size / 8;
     p.page_magic = p.page_groups > 1 ? (unsigned)(((1ull << 32) + p.page_groups - 1) / p.page_groups) : 0;
-    p.warp_share_log = 2;
-    p.cta_share_log = 2;
-    p.warp_parts = 3;
-    p.warp_extra = 1;
-    p.cta_extra = d.head_dim * kv->ces >= 512 ? 6 : 12;  // about 2 us of a CTA's share of the bandwidth; 8 KB tiles, else 16 KB
+    p.warp_share_log = p.cta_share_log = kKvShareLog;
+    p.warp_parts = kKvWarpParts;
+    p.warp_extra = kKvWarpExtra;
+    p.cta_extra = kv_cta_extra(d.head_dim * kv->ces);
     p.part = kv->part;
     p.part_ml = kv->part_ml;
     p.arrivals = kv->arrivals;

@@ -18,6 +18,10 @@ constexpr int kKvMaxB = 1024;      // requests a run (their tile counts are scan
 constexpr int kKvMaxSplits = 2;    // partial results a team can leave: of its first and its last segment
 constexpr int kKvAttnWarps = 4;
 constexpr int kKvJoin = 16;        // parts that are joined at a time
+constexpr int kKvShareLog = 2;     // log2 of the tiles that a team takes at least
+constexpr int kKvWarpParts = 3;    // teams are warps while no segment has more than this many of their shares
+constexpr int kKvWarpExtra = 1;    // numbers before a segment's tiles: for teams of a warp, and of a CTA,
+KV_HD constexpr int kv_cta_extra(int row_bytes) { return row_bytes >= 512 ? 6 : 12; }  // about 2 us of its share of the bandwidth (tiles of 16 KB, else 8)
 // Query heads of one unit: two n = 8 tensor-core tiles.  Over 256 dims in e4m3 one: two need more registers than a warp
 // has, and to read a KV head twice is faster (32 x 512..4096, 64 / 4 heads: 83 -> 59 us, 128 x 2048 232 -> 209, 8 x 30000
 // 155 -> 159; with twice the bytes to read again it is slower: 245 -> 304 us).
@@ -75,6 +79,89 @@ KV_HD int kv_share_teams(long long N, int most, int share_log) {
 KV_HD int kv_share_slot(long long c, long long s0, long long N, long long C) {
     return s0 <= kv_share_begin(c, N, C) ? 0 : 1;
 }
+
+// How a run's tiles are shared out: teams of one warp each (solo) or of a CTA each, C of them, that share N numbers, of
+// which `extra` before each segment's tiles stand for what its end costs (its join and the next one's start).
+struct KvTeams {
+    bool solo;
+    int extra, C;
+    long long N;
+};
+// tiles: of the n_live requests that have any, one KV head each; longest: the most of one
+KV_HD KvTeams kv_choose_teams(int tiles, int n_live, int longest, int units, int grid, int warps, int warp_share_log, int cta_share_log,
+                              int warp_extra, int cta_extra, int warp_parts) {
+    KvTeams t;
+    const long long n1 = (long long)(tiles + n_live * warp_extra) * units;
+    const int C1 = kv_share_teams(n1, grid * warps, warp_share_log);
+    t.solo = (long long)(longest + warp_extra) * C1 <= (long long)warp_parts * n1;
+    t.extra = t.solo ? warp_extra : cta_extra;
+    t.N = t.solo ? n1 : (long long)(tiles + n_live * t.extra) * units;
+    t.C = t.solo ? C1 : kv_share_teams(t.N, grid, cta_share_log);
+    // requests of one length: whole teams a segment, if few idle for it (a team with two segments takes twice as
+    // long in a small run: 1 x 517 11 -> 8 us)
+    const int segs = n_live * units;
+    if (t.N == (long long)(longest + t.extra) * segs && t.C >= segs && t.C % segs * 8 <= t.C) t.C -= t.C % segs;
+    return t;
+}
+
+// largest i < live with (pre[i] + i extra) units <= t: the request of numbered tile t
+KV_HD int kv_find_request(const int* pre, int live, int extra, int units, long long t) {
+    int lo = 0, hi = live;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)(pre[mid] + mid * extra) * units <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+// A segment, and its tiles counted from the first number of the team's run.
+struct KvWalk {
+    int i, u, nt;         // request (in the list of those that have tiles), unit, tiles of the segment
+    int s0, s1;           // [s0, s1): the segment's tiles
+};
+// the segment whose tiles, or the `extra` numbers before them, hold number t0
+KV_HD void kv_walk_to(KvWalk& w, const int* pre, int live, int extra, int units, long long t0) {
+    w.i = kv_find_request(pre, live, extra, units, t0);
+    w.nt = pre[w.i + 1] - pre[w.i];
+    const int r = (int)(t0 - (long long)(pre[w.i] + w.i * extra) * units);
+    w.u = r / (w.nt + extra);
+    w.s0 = w.u * (w.nt + extra) + extra - r;
+    w.s1 = w.s0 + w.nt;
+}
+// the next one; past the last segment it lies beyond every run
+KV_HD void kv_walk_next(KvWalk& w, const int* pre, int live, int extra, int units) {
+    w.s0 = w.s1 + extra;
+    if (++w.u == units) {
+        w.u = 0;
+        if (++w.i == live) {
+            w.s0 = 0x7FFFFFF0;
+            w.nt = 0;
+        } else {
+            w.nt = pre[w.i + 1] - pre[w.i];
+        }
+    }
+    w.s1 = w.s0 + w.nt;
+}
+
+// The parts of a shared segment: who leaves them, and where.
+struct KvParts {
+    int c0, n;            // the first team, how many
+    int first;            // which of its slots the first one uses; the others use slot 0
+};
+KV_HD KvParts kv_parts(long long s0, long long s1, long long N, int C) {  // [s0, s1): the segment's tiles, by number
+    KvParts p;
+    p.c0 = (int)kv_share_owner(s0, N, C);
+    p.n = (int)kv_share_owner(s1 - 1, N, C) - p.c0 + 1;
+    p.first = kv_share_slot(p.c0, s0, N, C);
+    return p;
+}
+KV_HD long long kv_part_slot(const KvParts& p, int k) { return (long long)(p.c0 + k) * kKvMaxSplits + (k == 0 ? p.first : 0); }
+// The join of a group of kKvJoin parts lies past the slots of the grid's CTAs, by the slot of the team that made it (a CTA may
+// do so for two segments).
+KV_HD long long kv_group_slot(int grid, long long slot) { return (long long)grid * kKvMaxSplits + slot; }
+KV_HD int kv_join_groups(int n_parts) { return (n_parts + kKvJoin - 1) / kKvJoin; }
+// what a handle allocates: slots, and events a segment (its own, then its groups')
+KV_HD long long kv_part_slots(int n_sm) { return 2ll * n_sm * kKvAttnWarps * kKvMaxSplits; }  // two CTAs an SM at most
+KV_HD int kv_arrivals(int n_sm) { return 1 + kv_join_groups(2 * n_sm); }
 
 // A length that can be used, or -1.
 KV_HD int kv_checked_len(int len, int max_len) { return len >= 0 && len <= max_len ? len : -1; }

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
     const bool fours = p.pool.page_size % 4 == 0 && (reinterpret_cast<uintptr_t>(p.pool.acc) & 15) == 0;
     const long long N = (long long)pre[live.n] * p.n_kv;
     for (long long t = blockIdx.x; t < N; t += gridDim.x) {
-        const int i = kv::find_request(pre, live.n, 0, p.n_kv, t), b = id[i];
+        const int i = kv_find_request(pre, live.n, 0, p.n_kv, t), b = id[i];
         const int nt = pre[i + 1] - pre[i];
         const int r = (int)(t - (long long)pre[i] * p.n_kv), u = r / nt;
         const int* pages = p.table.pages + (long long)b * p.table.ld;

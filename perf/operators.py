@@ -9,6 +9,7 @@ numbers a request):
 `own = False` runs the plain forms in torch, `own = True` the library's entry points.
 """
 import math
+import weakref
 
 import numpy as np
 import torch
@@ -190,9 +191,7 @@ class _Kv:
 
     def __init__(self, et, *a, **k):
         self.et, self.h = et, et.et_build_kv(*a, **k)
-
-    def __del__(self):
-        self.et.et_destroy_kv(self.h)
+        weakref.finalize(self, et.et_destroy_kv, self.h)  # at the interpreter's end too, while the library is still there
 
 
 def _handle(s, n_pages):

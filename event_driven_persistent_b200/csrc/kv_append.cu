@@ -166,7 +166,8 @@ __device__ __forceinline__ void append_rows(const KvAppendParams& p, const Token
                 *reinterpret_cast<uint4*>(dst) = make_uint4(T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7]));
                 *reinterpret_cast<uint4*>(dst + HALF) = make_uint4(T::pack(y[0], y[1]), T::pack(y[2], y[3]), T::pack(y[4], y[5]), T::pack(y[6], y[7]));
             } else {
-                // one rounding, from fp32 to e4m3 (times the scale's reciprocal: two fp32 roundings before it, 2^-23 of the value)
+                // one rounding, from fp32 to e4m3 (times the scale's reciprocal: two fp32 roundings before it, 2^-23 of the value;
+                // a division costs 12 % on the long chunk above, 44 % with 16 / 16 heads)
                 const float inv = 1.f / (KIND == 1 ? p.pool.k_scale[h] : p.pool.v_scale[h]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {

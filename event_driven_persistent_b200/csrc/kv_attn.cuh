@@ -34,15 +34,16 @@
 // remainder (16 bits or more of p together), so that rounding p adds nothing next to
 // the output's own rounding; with up to four heads a group the remainder
 // rides in the columns that would be padding.  (One fp16 term, 2^-11 of p, where an e4m3 cache meets bf16
-// outputs would show where values cancel; it is no faster up to 8 heads a group, 112 against 113 us for the
-// 8 x 20000..65000 below, and 97 against 112 us with 16 heads of 128.)  An e4m3 cache is widened to
+// outputs would show where values cancel.  It saves 1 us of the 112 of the
+// 8 x 20000..65000 below, 8 of 132 at the power limit, and 15 of 112 of 8 x 30000 with 16 heads of 128 a group.)  An e4m3 cache is widened to
 // fp16 exactly; bf16 queries are then scaled by a power of two into fp16's range.
 //
 // Measured (32 query and 8 KV heads of 128 in bf16, pages of 16, unless said; a
-// copy reaches 6535 GB/s): 1 x 131071 tokens, pages of 32, 87 us (6140 GB/s);
-// 8 x 20000..65000, 64 heads, e4m3, pages of 64, 112 us (6200); 16 x 512..4096
-// 31 us (4930); 128 x 1..900, 16 / 16 heads of 64 in fp16, pages of 24, 46 us
-// (5100); 1 x 517 8 us, a chain of latencies.  Long or many tokens are bound
+// copy reaches 6535 GB/s): 1 x 131071 tokens, pages of 32, 88 us (6100 GB/s);
+// 8 x 20000..65000, 64 heads, e4m3, pages of 64, 112 us (6200; held for a
+// second the GPU meets its power limit, and at 1.8 GHz it is 132 us); 16 x 512..4096
+// 31 us (4870); 128 x 1..900, 16 / 16 heads of 64 in fp16, pages of 24, 47 us
+// (5030); 1 x 517 8 us, a chain of latencies.  Long or many tokens are bound
 // by HBM; what a run adds to that is about 5 us before its first tile and
 // 2 us for a segment that several teams share.
 #pragma once
@@ -114,6 +115,7 @@ attn_kernel(const __grid_constant__ KvAttnParams p) {
     const int units = p.n_kv * p.n_qt;
 
     grid_wait();
+    // (the weights kernel, if any, counts on the release below lying behind this wait)
     const Live live = scan_tiles<W * 32>(pre, id, tmp, p.lens, p.B, KT, p.table.max_len, p.ctl);
     grid_launch();
 

@@ -201,8 +201,11 @@ __device__ __forceinline__ Live scan_tiles(int* pre, uint16_t* id, int* tmp, con
 }
 
 // Launch with programmatic serialisation: the grid may be set up while the
-// one before it drains; every kernel here calls grid_wait() before it reads
-// or writes anything another launch touches.
+// one before it drains.  Every kernel here calls grid_wait() before it reads
+// or writes anything another launch touches, but for the weights kernel: it
+// reads the lengths (and reports a bad one) before.  That is sound because the
+// attention it follows releases it behind a grid_wait() of its own: whoever
+// wrote the lengths is done by then.
 template <class... P>
 cudaError_t launch_pdl(void (*f)(P...), dim3 grid, dim3 block, int smem, cudaStream_t s, int cluster, P... args) {
     cudaLaunchConfig_t cfg = {};

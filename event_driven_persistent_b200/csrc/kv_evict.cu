@@ -5,9 +5,11 @@
 // Two launches, the selection and the move: no row may move before every
 // destination page has been claimed, and in place a row's slot may be written once it has been read.
 // Bound: memory; the weights are read once, the kept rows read and written once.
-// Measured (8 KV heads of 128): 32 requests of 1500..4096 slots to 2048 in bf16 97 us, of which the
-// selection takes 10 and the move reaches 6000 GB/s; 4 x 65537 to 8192 in e4m3 46.5 us, 20 of them the
-// selection: two passes of counting and five barriers across a cluster of eight CTAs; 1 x 4096 to 1024 10.3 us, latency.
+// Measured (8 KV heads of 128), to other pages: 32 requests of 1500..4096 slots to 2048 in bf16 97.5 us, of which the
+// selection takes 10 and the move reaches 6000 GB/s; 4 x 65537 to 8192 in e4m3 47 us, 20 of them the
+// selection: two passes of counting and five barriers across a cluster of eight CTAs; 1 x 4096 to 1024 10.6 us, latency.
+// In place: 91 us, 113 us and 17 us; 1 x 65537 to 8192 in bf16 106 us (to other pages 31): few CTAs walk each row's tiles
+// in order, each tile a chain of memory latencies.
 #include <cooperative_groups.h>
 
 #include "kv_device.cuh"
@@ -484,9 +486,11 @@ cudaError_t setup_kv_evict() {
 }
 cudaError_t launch_kv_evict(const KvEvictParams& p, int n_sm, cudaStream_t s) {
     using namespace kv;
-    // CTAs a row: as many as keep a slice within 4096 slots, while they fit the GPU at two an SM (16 x 16384, 8 heads:
-    // 65 us, with four an SM, which come in two waves, 74).  Short rows take
-    // CTAs of 128 threads, of which many fit an SM (79 requests of 800 slots, 8 heads: 24 -> 16 us).
+    // By the longest row that the handle and the table hold, since the host does not know the lengths.  CTAs a row: as many as
+    // keep a slice within 4096 slots, while they fit the GPU at two an SM (16 x 16384, 8 heads: 65 us, with four an SM, which
+    // come in two waves, 74).  Short rows take CTAs of 128 threads, of which many fit an SM (the selection of 79 requests of 800
+    // slots, 8 heads: 24 -> 16 us).  A handle and table for 131072 slots give short rows more CTAs or larger ones than
+    // they need: 79 x 800 to 400 64 us in place of 56, 1 x 4096 to 1024 13 in place of 10.6; 32 x 1500..4096 98, as with its own.
     int cs = 1;
     while (cs < 8 && p.src.max_len / cs > 4096 && (long long)p.B * p.n_kv * cs * 2 <= 2 * n_sm) cs *= 2;
     int cap = ((p.src.max_len + cs - 1) / cs + 3) & ~3;

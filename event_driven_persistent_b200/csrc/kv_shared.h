@@ -23,8 +23,10 @@ constexpr int kKvWarpParts = 3;    // teams are warps while no segment has more 
 constexpr int kKvWarpExtra = 1;    // numbers before a segment's tiles: for teams of a warp, and of a CTA,
 KV_HD constexpr int kv_cta_extra(int row_bytes) { return row_bytes >= 512 ? 6 : 12; }  // about 2 us of its share of the bandwidth (tiles of 16 KB, else 8)
 // Query heads of one unit: two n = 8 tensor-core tiles.  Over 256 dims in e4m3 one: two need more registers than a warp
-// has, and to read a KV head twice is faster (32 x 512..4096, 64 / 4 heads: 83 -> 59 us, 128 x 2048 232 -> 209, 8 x 30000
-// 155 -> 159; with twice the bytes to read again it is slower: 245 -> 304 us).
+// has (340 bytes spilled), and to read a KV head twice is faster where there are many ends or joins, slower over long rows.
+// 64 / 4 heads, units of 16 and of 8: 32 x 512..4096 82 and 60 us, 128 x 2048 229 and 197, 1 x 60000 76 and 63, 8 x 30000
+// 152 and 157 (held for seconds, at the power limit's clocks, 152 and 180).  With twice the bytes to read again, in bf16, it
+// is slower: 8 x 30000 245 and 304.
 KV_HD constexpr int kv_unit_heads(int hd, bool e4m3) { return hd == 256 && e4m3 ? 8 : 16; }
 
 // Where the error of a run is kept; the first one stays until it is collected.
@@ -33,7 +35,7 @@ struct KvCtl {
     int diag[8];
     int* host_status;        // mapped host word the status is mirrored into
     unsigned evict_run;      // number of the current eviction (tags the page owners)
-    unsigned evict_done;     // CTAs of the eviction's last kernel that are done
+    unsigned evict_done;     // CTAs of the eviction's selection that are done
 };
 // diag[0] of a KvCtl: what was out of range
 enum { KV_BAD_LEN = 1, KV_BAD_PAGE = 2, KV_BAD_REQ = 3, KV_BAD_SLOT = 4, KV_BAD_DST = 5, KV_BAD_WEIGHT = 6 };

@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
     __shared__ int tmp[2 * kThreads / 32];
     __shared__ uint16_t id[kKvMaxB];
     extern __shared__ int pre[];
+    // before the wait: the lengths are done where the attention before this kernel has released it (its release is behind its own wait)
     const kv::Live live = kv::scan_tiles<kThreads>(pre, id, tmp, p.lens, p.B, kSlots, p.table.max_len, ctl);
     kv::grid_wait();
     const bool fours = p.pool.page_size % 4 == 0 && (reinterpret_cast<uintptr_t>(p.pool.acc) & 15) == 0;

@@ -447,7 +447,7 @@ typedef struct {
     int head_dim;        /* 64, 128 or 256 [128] */
     int dtype;           /* of queries, new keys and values, outputs, gains: ET_BF16 or ET_FP16 */
     int cache_dtype;     /* of the pools: dtype, or ET_E4M3 (8 bits, a scale per KV head) */
-    int track_weights;   /* 1: runs may record attention weights (workspace for max_B * n_heads * max_ctx scores) */
+    int track_weights;   /* 1: runs may record attention weights (workspace: 4 * max_B * n_heads * max_ctx bytes) */
     float rope_base;     /* [500000] */
     float rms_eps;       /* [1e-5] */
 } et_kv_desc;
@@ -479,8 +479,10 @@ void et_destroy_kv(et_kv* kv);
  *   y  = x * rsqrt(mean(x^2) + rms_eps) * gain   per head, if a gain is given
  *   z  = rope(y, pos[n])                         if pos is given (pairs i, i + head_dim/2, as et_run_decode)
  *   q_out = round(z of q);  K slot = round(z of k / k_scale);  V slot = round(v / v_scale)
- * (scales with ET_E4M3 only; that rounding is to nearest even and saturates at
- * 448).  q [N, n_heads, head_dim], k and v [N, n_kv_heads, head_dim], each
+ * (scales with ET_E4M3 only, fp32 numbers whose reciprocals are normal: the
+ * quotient is the product with the rounded reciprocal, within 2^-23 of itself,
+ * so a value that lies so close to the middle of two e4m3 values may go to
+ * either; that rounding is to nearest even and saturates at 448).  q [N, n_heads, head_dim], k and v [N, n_kv_heads, head_dim], each
  * with its row stride in elements (multiples of 8: slices of one fused
  * projection serve); q and q_out may be NULL, or the same (q_out overlaps
  * neither k nor v).  pool->acc, if given, is zeroed at the new slots.  Rows of one run that name the same slot
@@ -512,7 +514,9 @@ et_status et_run_kv_append(et_kv* kv, const et_kv_pool* pool, const et_kv_append
  * scale 0 = 1 / sqrt(head_dim).  q and out [B, n_heads, head_dim] with row
  * strides in elements (multiples of 8); lse fp32 [B, n_heads] or NULL.
  * lens[b] = 0: out = 0, lse = -inf.  Infinite and NaN keys give what the formula
- * gives; an attended infinity in V gives NaN.  accumulate = 1 (needs track_weights and
+ * gives; an attended infinity in V makes its dim of the output infinite or
+ * NaN (probabilities are multiplied as a sum of two terms, one of which may be
+ * 0 or negative), the other dims as the formula gives.  accumulate = 1 (needs track_weights and
  * pool->acc): acc of each slot += the softmax weight it got, summed over the
  * query heads of the KV head.  Requests may share pages.  The result does not
  * depend on timing (with shared pages, acc's last bits may). */
@@ -545,7 +549,9 @@ et_status et_run_kv_attn(et_kv* kv, const et_kv_pool* pool, const et_kv_attn_arg
  * different choices: then nothing moves.
  * new_lens int32 [B] (may be lens): min(lens[b], budget); kept int32 [B,
  * n_kv_heads, budget]: the old slot of each new one, -1 past new_lens[b].
- * 1 <= budget, n_recent + n_sink <= budget. */
+ * 1 <= budget, n_recent + n_sink <= budget.  In place a row is moved by few
+ * CTAs one part after another, which takes longer than a move to other pages
+ * where rows are few and long. */
 typedef struct {
     const int32_t* table;      /* [B, ld_table] */
     int64_t ld_table;

@@ -210,7 +210,7 @@ et_status et_build_kv(const et_kv_desc* desc, et_kv** out) {
         int major = 0;
         if (on.ok && cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d.device) == cudaSuccess &&
             cudaDeviceGetAttribute(&kv->n_sm, cudaDevAttrMultiProcessorCount, d.device) == cudaSuccess) {
-            if (major != 10) {
+            if (major != 10 || kv_longest_run(d.max_B, d.max_ctx, d.n_kv_heads * kv->n_qt, kv->n_sm) >= 1 << 30) {
                 st = ET_ERR_UNSUPPORTED;
             } else {
                 try {

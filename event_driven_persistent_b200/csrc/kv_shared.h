@@ -106,6 +106,12 @@ KV_HD KvTeams kv_choose_teams(int tiles, int n_live, int longest, int units, int
     return t;
 }
 
+// An upper bound of the numbers that one team takes, for a handle's longest possible run: a team counts its own in 32 bits.
+KV_HD long long kv_longest_run(int max_B, int max_ctx, int units, int n_sm) {
+    const long long N = (long long)max_B * ((max_ctx + 15) / 16 + 12) * units;  // tiles have 16 keys or more
+    return N / n_sm / 7 * 8 + 8;  // one CTA an SM at least, of which an eighth may idle
+}
+
 // largest i < live with (pre[i] + i extra) units <= t: the request of numbered tile t
 KV_HD int kv_find_request(const int* pre, int live, int extra, int units, long long t) {
     int lo = 0, hi = live;

@@ -438,7 +438,8 @@ typedef enum { ET_BF16 = 0, ET_FP16 = 1, ET_E4M3 = 2 } et_dtype;
 typedef struct {
     int device;          /* CUDA device ordinal */
     int max_B;           /* requests a run, up to 1024 */
-    int max_ctx;         /* slots a request, up to 2^24 */
+    int max_ctx;         /* slots a request, up to 2^24; max_B * max_ctx * n_kv_heads (counted once for every 16 query
+                            heads of one, 8 over 256 dims in ET_E4M3) below about 2^41: a run's tiles are counted in 32 bits an SM */
     int n_pages;         /* pages of the pools */
     /* 0 = the default in brackets */
     int page_size;       /* slots a page, 1 to 4096 [16] */

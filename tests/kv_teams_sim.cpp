@@ -44,7 +44,7 @@ int main(int argc, char** argv) {
     for (int c = 0; c < t.C; ++c) {
         const long long share = kv_share_div(t.N, t.C), t0 = kv_share_begin(c, t.N, t.C, share), t1 = kv_share_begin(c + 1, t.N, t.C, share);
         const int run = (int)(t1 - t0), team = t.solo ? 1 : warps;
-        CHECK(run > 0);
+        CHECK(run > 0 && run <= kv_longest_run(argc - 6, longest * tile, units, n_sm));
         std::vector<std::vector<std::pair<int, int>>> loads(team), uses(team);  // by warp: (segment's first number, tile counted from t0)
         for (int tw = 0; tw < team; ++tw) {
             KvWalk lw;

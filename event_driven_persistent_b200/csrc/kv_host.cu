@@ -1,6 +1,7 @@
 // Host half of the paged key-value cache: its C entry points (include/et.h),
 // checks of arguments, workspace and launches.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -292,7 +293,7 @@ et_status et_run_kv_attn(et_kv* kv, const et_kv_pool* pool, const et_kv_attn_arg
     if (!al4(a->lens) || !al16(a->q) || !al16(a->out) || bad_ld(a->ldq) || bad_ld(a->ldo) || (a->lse && !al4(a->lse)))
         return ET_ERR_INVALID;
     if (a->B > 1 && a->ldo < (int64_t)d.n_heads * d.head_dim) return ET_ERR_INVALID;  // rows of the output would overlap
-    if (!(scale >= 0.f) || !(scale < INFINITY)) return ET_ERR_INVALID;
+    if (!(scale >= 0.f) || !(scale * 1.4426950408889634 <= FLT_MAX)) return ET_ERR_INVALID;  // the kernel's scale is log2(e) of it
     if (accumulate && (!pool->acc || !kv->scores)) return ET_ERR_INVALID;
     KV_TRY(not_pending(kv));
     OnDevice on(d.device);

@@ -512,7 +512,7 @@ et_status et_run_kv_append(et_kv* kv, const et_kv_pool* pool, const et_kv_append
 /* Attention of one new token a request over slots 0 .. lens[b] - 1, query
  * head h reading KV head h / (n_heads / n_kv_heads):
  *   out[b,h] = sum_j softmax_j(scale q_h . K_j) V_j,  lse[b,h] = log sum_j exp(scale q_h . K_j)
- * scale 0 = 1 / sqrt(head_dim).  q and out [B, n_heads, head_dim] with row
+ * scale 0 = 1 / sqrt(head_dim); scale * log2(e) is finite in fp32.  q and out [B, n_heads, head_dim] with row
  * strides in elements (multiples of 8); lse fp32 [B, n_heads] or NULL.
  * lens[b] = 0: out = 0, lse = -inf.  Infinite and NaN keys give what the formula
  * gives; an attended infinity in V makes its dim of the output infinite or
